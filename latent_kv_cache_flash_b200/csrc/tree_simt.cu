@@ -55,8 +55,9 @@ template <typename T, int kU>
 __global__ void __launch_bounds__(kThreads, kU == 1 ? 3 : kU == 2 ? 2 : 1)
     tree_simt_kernel(const SimtParams p, const float* __restrict__ qa, const T* __restrict__ qb, int q_skip,
                      const T* __restrict__ kpool, const T* __restrict__ vpool) {
-  // after the query lift, only its result has to be waited for: that kernel
-  // started when all before it had ended
+  // After the query lift (latent form), only its result has to be waited for:
+  // that kernel started when all before it had ended.  Without one, the kernel
+  // ahead may be what writes the lengths, sizes or pages.
   if (qa == nullptr) ptx::pdl_wait();
   ptx::pdl_trigger();
   extern __shared__ __align__(16) float sm[];
@@ -160,7 +161,8 @@ __global__ void __launch_bounds__(kThreads, kU == 1 ? 3 : kU == 2 ? 2 : 1)
 #pragma unroll
       for (int k = 0; k < kTok / 4; ++k) {
         const int t = (tid >> 6) + 4 * k;
-        vx[k] = t0 + t < t_end && ((any >> t) & 1) && col < p.dv ? vpool[s_row[t] * p.vrs + voff + col] : T(0.f);
+        const long long row = s_row[t];
+        vx[k] = row >= 0 && t0 + t < t_end && ((any >> t) & 1) && col < p.dv ? vpool[row * p.vrs + voff + col] : T(0.f);
       }
     };
     load_values(0);
@@ -432,7 +434,7 @@ cudaError_t run(const Problem& p, const TreeView& tree, gqla_path path, const Si
                 cudaStream_t s) {
   const auto& d = p.d;
   const bool lat = path == GQLA_PATH_ABSORB;
-  float* qt = (float*)(ws + w.qt);
+  float* qt = lat ? (float*)(ws + w.qt) : nullptr;      // nullptr: no query lift runs ahead
   cudaError_t e = cudaSuccess;
   if (lat) e = launch_lift<T, T, float, true>(p, (const T*)q, p.d_qk, W_uk, qt, d.d_nope, d.r, s);
   if (e != cudaSuccess) return e;
