@@ -9,6 +9,7 @@ There is no fallback: if the library is missing, loading raises.
 from __future__ import annotations
 
 import array
+import contextlib
 import ctypes
 import math
 import operator
@@ -125,6 +126,19 @@ def _stream(stream, device):
     return None
 
 
+def _allocating_on(stream, device):
+    """Context in which a call's own workspace is allocated: torch hands a
+    freed block to later allocations of the same stream, so it has to belong
+    to the stream whose kernels still use it when the call returns."""
+    if stream is None or device.type != "cuda":
+        return contextlib.nullcontext()
+    handle = getattr(stream, "value", stream) or 0
+    if handle == torch.cuda.current_stream(device).cuda_stream:
+        return contextlib.nullcontext()
+    # torch takes an external handle of 0 for none
+    return torch.cuda.stream(torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device))
+
+
 def _check(status: int, what: str):
     if status != GQLA_OK:
         raise GqlaError(status, "%s: %s" % (what, gqla_status_string(status)))
@@ -221,7 +235,8 @@ def gqla_decode_absorb(dims, layout, q, latent, W_uk, W_uv, out, lse=None, num_s
     fp32 (natural log) when given.  num_splits 0 takes the library's plan; a
     workspace of gqla_workspace_bytes is allocated when none is passed."""
     if workspace is None:
-        workspace = workspace_for(dims, layout, num_splits, GQLA_PATH_ABSORB, q.device)
+        with _allocating_on(stream, q.device):
+            workspace = workspace_for(dims, layout, num_splits, GQLA_PATH_ABSORB, q.device)
     s = lib().gqla_decode_absorb(ctypes.byref(dims), ctypes.byref(layout), _ptr(q), _ptr(latent), _ptr(W_uk),
                                  _ptr(W_uv), _ptr(out), _ptr(lse), int(num_splits), _ptr(workspace),
                                  workspace.numel() * workspace.element_size(), _ptr(dev_status),
@@ -235,7 +250,8 @@ def gqla_decode_gqa(dims, layout, q, k_pool, v_pool, out, lse=None, num_splits=0
     attend to that group's K/V rows.  Same output, lse, split and workspace
     conventions as gqla_decode_absorb."""
     if workspace is None:
-        workspace = workspace_for(dims, layout, num_splits, GQLA_PATH_GQA, q.device)
+        with _allocating_on(stream, q.device):
+            workspace = workspace_for(dims, layout, num_splits, GQLA_PATH_GQA, q.device)
     s = lib().gqla_decode_gqa(ctypes.byref(dims), ctypes.byref(layout), _ptr(q), _ptr(k_pool), _ptr(v_pool),
                               _ptr(out), _ptr(lse), int(num_splits), _ptr(workspace),
                               workspace.numel() * workspace.element_size(), _ptr(dev_status),
@@ -348,7 +364,8 @@ def gqla_decode_tree_gqa(dims, layout, tree, q, k_pool, v_pool, out, lse=None, n
     [B, s_q, n_h]; rows of slots past a sequence's tree are 0 and -inf.
     num_splits is used by the forms without tensor cores only."""
     if workspace is None:
-        workspace = tree_workspace_for(dims, layout, num_splits, GQLA_PATH_GQA, q.device)
+        with _allocating_on(stream, q.device):
+            workspace = tree_workspace_for(dims, layout, num_splits, GQLA_PATH_GQA, q.device)
     _call("gqla_decode_tree_gqa", lib().gqla_decode_tree_gqa, q, stream, ctypes.byref(dims), ctypes.byref(layout),
           ctypes.byref(tree), _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(out), _ptr(lse), int(num_splits),
           _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(dev_status))
@@ -359,7 +376,8 @@ def gqla_decode_tree_absorb(dims, layout, tree, q, latent, W_uk, W_uv, out, lse=
     """Attention of a tree of drafted tokens over the latent pool (the
     absorbed form); otherwise as gqla_decode_tree_gqa."""
     if workspace is None:
-        workspace = tree_workspace_for(dims, layout, num_splits, GQLA_PATH_ABSORB, q.device)
+        with _allocating_on(stream, q.device):
+            workspace = tree_workspace_for(dims, layout, num_splits, GQLA_PATH_ABSORB, q.device)
     _call("gqla_decode_tree_absorb", lib().gqla_decode_tree_absorb, q, stream, ctypes.byref(dims),
           ctypes.byref(layout), ctypes.byref(tree), _ptr(q), _ptr(latent), _ptr(W_uk), _ptr(W_uv), _ptr(out),
           _ptr(lse), int(num_splits), _ptr(workspace), workspace.numel() * workspace.element_size(),
