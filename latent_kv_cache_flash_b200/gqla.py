@@ -160,8 +160,10 @@ def make_layout(seq_lens: torch.Tensor, max_seq_len: int, page_size: int = 0, ca
                 block_table: Optional[torch.Tensor] = None, num_pages: int = 0) -> GqlaKvLayout:
     """seq_lens and block_table are int32 device tensors (kept alive by the caller)."""
     mbps = 0 if block_table is None else int(block_table.shape[1])
-    return GqlaKvLayout(int(seq_lens.shape[0]), _ptr(seq_lens), int(max_seq_len), int(page_size),
-                        int(capacity), _ptr(block_table), mbps, int(num_pages))
+    lay = GqlaKvLayout(int(seq_lens.shape[0]), _ptr(seq_lens), int(max_seq_len), int(page_size),
+                       int(capacity), _ptr(block_table), mbps, int(num_pages))
+    lay._device = seq_lens.get_device()
+    return lay
 
 
 def gqla_status_string(status: int) -> str:
@@ -285,10 +287,68 @@ def _require(cond: bool, what: str):
         raise ValueError(what)
 
 
-def _plain(t: Optional[torch.Tensor], dtype, shape, name: str):
-    """A contiguous tensor of this type and shape, or None."""
-    if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        raise ValueError("%s: contiguous %s %s expected" % (name, dtype, list(shape)))
+def _plain(t: Optional[torch.Tensor], dtype, shape, dev: int, name: str):
+    """A contiguous tensor of this type and shape on this device, or None."""
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == dev):
+        raise ValueError("%s: contiguous %s %s on the call's device expected" % (name, dtype, list(shape)))
+
+
+def _dense(dev: int, expected):
+    """Contiguous tensors on this device; expected: (tensor, dtype, elements,
+    name), a negative number for "at least"; a tensor may be None."""
+    for t, dtype, n, name in expected:
+        if t is None:
+            continue
+        size = t.numel()
+        if not ((size == n or 0 <= -n <= size) and t.dtype is dtype and t.is_contiguous() and t.get_device() == dev):
+            raise ValueError("%s: %s%d contiguous elements of %s on the call's device expected" %
+                             (name, "at least " if n < 0 else "", abs(n), dtype))
+
+
+def _status(t: Optional[torch.Tensor], dev: int):
+    if t is not None:
+        _dense(dev, ((t, torch.int32, -1, "dev_status"),))
+
+
+def _on_layouts_device(layout, dev: int):
+    if getattr(layout, "_device", dev) != dev:
+        raise ValueError("layout: lengths on the call's device expected")
+
+
+def _rows(layout) -> int:
+    """Token rows of a pool."""
+    per = layout.page_size
+    return layout.num_pages * per if per else layout.batch * layout.capacity
+
+
+def _element(dims):
+    return torch.float32 if dims.dtype == GQLA_F32 else torch.bfloat16
+
+
+def _expanded(dims, dt, rows: int, k_pool, v_pool):
+    G, r = dims.G, dims.d_rope
+    return ((k_pool, dt, -rows * (G * dims.d_nope + (r if dims.k_layout == GQLA_K_SHARED_ROPE else G * r)), "k_pool"),
+            (v_pool, dt, -rows * G * dims.d_v, "v_pool"))
+
+
+def _weights(dims, dt, W_uk, W_uv):
+    per = dims.G * dims.r
+    return (W_uk, dt, per * dims.d_nope, "W_uk"), (W_uv, dt, per * dims.d_v, "W_uv")
+
+
+def _attention(dims, dt, layout, tree, q, out, lse, workspace, dev_status, model):
+    """Checks the tensors of a tree attention call."""
+    dev = q.get_device()
+    _on_layouts_device(layout, dev)
+    B, T = layout.batch, dims.s_q
+    slots = getattr(tree, "_slots", None)
+    if slots is not None and slots != (B, T, dev):
+        raise ValueError("tree: masks [%d, %d] on the call's device expected" % (B, T))
+    rows = B * T * dims.n_h
+    _dense(dev, ((q, dt, rows * (dims.d_nope + dims.d_rope), "q"), (out, dt, rows * dims.d_v, "out"),
+                 (lse, torch.float32, rows, "lse"), (dev_status, torch.int32, -1, "dev_status")) + model)
+    if workspace is not None and (workspace.get_device() != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace: contiguous on the call's device expected")
 
 
 # The current stream's handle without a Stream object around it, which costs a
@@ -316,18 +376,23 @@ def make_tree(masks: torch.Tensor, sizes: Optional[torch.Tensor] = None) -> Gqla
     kept alive by the caller; sizes None: every sequence drafted s_q tokens."""
     _require(masks.dtype in (torch.int64, torch.uint64) and masks.dim() == 2 and masks.is_contiguous(),
              "masks: contiguous 64-bit words [batch, tokens] expected")
-    _plain(sizes, torch.int32, masks.shape[:1], "sizes")
-    return GqlaTree(_ptr(masks), _ptr(sizes))
+    dev = masks.get_device()
+    _plain(sizes, torch.int32, masks.shape[:1], dev, "sizes")
+    tree = GqlaTree(_ptr(masks), _ptr(sizes))
+    tree._slots = (*masks.shape, dev)
+    return tree
 
 
 def gqla_tree_masks(parents, masks, sizes=None, dev_status=None, stream=None):
     """masks[b, i] = bits of drafted token i and its ancestors, from
     parents [B, n_tokens] int32 (parents[b, i] < i, -1 for a root)."""
     _require(parents.dim() == 2, "parents: [batch, tokens] expected")
-    _plain(parents, torch.int32, parents.shape, "parents")
-    _plain(sizes, torch.int32, parents.shape[:1], "sizes")
-    _require(masks.dtype in (torch.int64, torch.uint64) and masks.shape == parents.shape and masks.is_contiguous(),
-             "masks: contiguous 64-bit words of the parents' shape expected")
+    dev = parents.get_device()
+    _plain(parents, torch.int32, parents.shape, dev, "parents")
+    _plain(sizes, torch.int32, parents.shape[:1], dev, "sizes")
+    _require(masks.dtype in (torch.int64, torch.uint64) and masks.shape == parents.shape and masks.is_contiguous() and
+             masks.get_device() == dev, "masks: contiguous 64-bit words of the parents' shape expected")
+    _status(dev_status, dev)
     B, T = parents.shape
     _call("gqla_tree_masks", lib().gqla_tree_masks, parents, stream, B, T, _ptr(parents), _ptr(sizes), _ptr(masks),
           _ptr(dev_status))
@@ -337,7 +402,14 @@ def gqla_append_tree(dims, layout, new_rows, latent, W_uk=None, W_uv=None, k_poo
                      dev_status=None, stream=None):
     """gqla_append_tokens for the drafted tokens: rows new_rows[b, i],
     i < sizes[b], go to positions seq_len - sizes[b] + i."""
-    _plain(sizes, torch.int32, (layout.batch,), "sizes")
+    dev = new_rows.get_device()
+    _on_layouts_device(layout, dev)
+    _plain(sizes, torch.int32, (layout.batch,), dev, "sizes")
+    dt, rows, width = _element(dims), _rows(layout), dims.r + dims.d_rope
+    _dense(dev, ((new_rows, dt, layout.batch * dims.s_q * width, "new_rows"), (latent, dt, -rows * width, "latent")))
+    if k_pool is not None or v_pool is not None:
+        _dense(dev, _expanded(dims, dt, rows, k_pool, v_pool) + _weights(dims, dt, W_uk, W_uv))
+    _status(dev_status, dev)
     _call("gqla_append_tree", lib().gqla_append_tree, new_rows, stream, ctypes.byref(dims), ctypes.byref(layout),
           _ptr(sizes), _ptr(new_rows), _ptr(latent), _ptr(W_uk), _ptr(W_uv), _ptr(k_pool), _ptr(v_pool),
           _ptr(dev_status))
@@ -363,6 +435,9 @@ def gqla_decode_tree_gqa(dims, layout, tree, q, k_pool, v_pool, out, lse=None, n
     drafted tokens of tree.masks[b, i].  out [B, s_q, n_h, d_v], lse
     [B, s_q, n_h]; rows of slots past a sequence's tree are 0 and -inf.
     num_splits is used by the forms without tensor cores only."""
+    dt = _element(dims)
+    _attention(dims, dt, layout, tree, q, out, lse, workspace, dev_status,
+               _expanded(dims, dt, _rows(layout), k_pool, v_pool))
     if workspace is None:
         with _allocating_on(stream, q.device):
             workspace = tree_workspace_for(dims, layout, num_splits, GQLA_PATH_GQA, q.device)
@@ -375,6 +450,9 @@ def gqla_decode_tree_absorb(dims, layout, tree, q, latent, W_uk, W_uv, out, lse=
                             dev_status=None, stream=None):
     """Attention of a tree of drafted tokens over the latent pool (the
     absorbed form); otherwise as gqla_decode_tree_gqa."""
+    dt = _element(dims)
+    _attention(dims, dt, layout, tree, q, out, lse, workspace, dev_status,
+               ((latent, dt, -_rows(layout) * (dims.r + dims.d_rope), "latent"),) + _weights(dims, dt, W_uk, W_uv))
     if workspace is None:
         with _allocating_on(stream, q.device):
             workspace = tree_workspace_for(dims, layout, num_splits, GQLA_PATH_ABSORB, q.device)
@@ -413,14 +491,17 @@ def gqla_verify_tree(parents, tokens, target, draft, u_accept, u_sample, accepte
              (draft is None or (draft.dtype is dt and draft.shape == shape)),
              "target and draft: both fp32 or both bf16 [batch, tokens, vocab] expected")
     slots, rows = shape[:2], shape[:1]
-    _plain(parents, i32, slots, "parents")
-    _plain(tokens, i32, slots, "tokens")
-    _plain(accepted, i32, slots, "accepted")
-    _plain(n_accepted, i32, rows, "n_accepted")
-    _plain(next_token, i32, rows, "next_token")
-    _plain(sizes, i32, rows, "sizes")
-    _plain(u_accept, torch.float32, slots, "u_accept")
-    _plain(u_sample, torch.float32, rows, "u_sample")
+    dev = target.get_device()
+    _require(draft is None or draft.get_device() == dev, "draft: the target's device expected")
+    _plain(parents, i32, slots, dev, "parents")
+    _plain(tokens, i32, slots, dev, "tokens")
+    _plain(accepted, i32, slots, dev, "accepted")
+    _plain(n_accepted, i32, rows, dev, "n_accepted")
+    _plain(next_token, i32, rows, dev, "next_token")
+    _plain(sizes, i32, rows, dev, "sizes")
+    _plain(u_accept, torch.float32, slots, dev, "u_accept")
+    _plain(u_sample, torch.float32, rows, dev, "u_sample")
+    _status(dev_status, dev)
     _call("gqla_verify_tree", lib().gqla_verify_tree, target, stream, B, T, V, _ptr(parents), _ptr(sizes), _ptr(tokens),
           _ptr(target), _pitch(target, B, T, V, "target"), _ptr(draft),
           0 if draft is None else _pitch(draft, B, T, V, "draft"),
@@ -439,10 +520,13 @@ def gqla_commit_tree(layout, accepted, n_accepted, pools, seq_lens_out=None, siz
     B, T = accepted.shape
     _require(B == layout.batch, "accepted: the layout's batch expected")
     i32, rows = torch.int32, accepted.shape[:1]
-    _plain(accepted, i32, (B, T), "accepted")
-    _plain(n_accepted, i32, rows, "n_accepted")
-    _plain(seq_lens_out, i32, rows, "seq_lens_out")
-    _plain(sizes, i32, rows, "sizes")
+    dev = accepted.get_device()
+    _on_layouts_device(layout, dev)
+    _plain(accepted, i32, (B, T), dev, "accepted")
+    _plain(n_accepted, i32, rows, dev, "n_accepted")
+    _plain(seq_lens_out, i32, rows, dev, "seq_lens_out")
+    _plain(sizes, i32, rows, dev, "sizes")
+    _status(dev_status, dev)
     lead = (B, layout.capacity) if layout.page_size == 0 else (layout.num_pages, layout.page_size)
     # the pools of a model's layers are alike, and there are many
     shapes = list(map(_shape, pools))
@@ -452,6 +536,7 @@ def gqla_commit_tree(layout, accepted, n_accepted, pools, seq_lens_out=None, siz
     _require(all(len(shape) >= 3 and shape[:2] == lead for shape in (shapes[:1] if alike else shapes)),
              "pools: [%d, %d, ...] of the layout expected" % lead)
     _require(all(map(torch.Tensor.is_contiguous, pools)), "pools: contiguous tensors expected")
+    _require(list(map(torch.Tensor.get_device, pools)).count(dev) == n, "pools: the path's device expected")
     flat = [0] * (2 * n)
     flat[0::2] = map(torch.Tensor.data_ptr, pools)
     flat[1::2] = ([math.prod(shapes[0][2:]) * sizes_of[0]] * n if alike else

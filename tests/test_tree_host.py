@@ -172,3 +172,52 @@ def test_reference_sampling_keeps_the_targets_law(shape):
         count[tokens[path[1]] if len(path) > 1 else nxt] += 1
     for v, p in enumerate(target[0]):
         assert abs(count[v] - trials * p) < 5 * (trials * p * (1 - p)) ** 0.5
+
+
+def _attention_args(G, path, dtype=torch.bfloat16, page=0, shared=0):
+    B, T, h, g, n, r, v, R, L = 2, 3, 4, 2, 16, 8, 24, 32, 64
+    d = G.GqlaDims(h, g, n, r, v, R, T, 0.1, G.GQLA_BF16 if dtype is torch.bfloat16 else G.GQLA_F32, shared)
+    lens = torch.full((B,), 10, dtype=torch.int32)
+    lead = (5, page) if page else (B, L)
+    table = torch.zeros((B, 2), dtype=torch.int32) if page else None
+    lay = G.make_layout(lens, L, page, 0 if page else L, table, 5 if page else 0)
+    a = dict(dims=d, layout=lay, tree=G.make_tree(torch.zeros((B, T), dtype=torch.int64)),
+             q=torch.zeros((B, T, h, n + r), dtype=dtype), out=torch.zeros((B, T, h, v), dtype=dtype),
+             lse=torch.zeros((B, T, h)))
+    weights = dict(W_uk=torch.zeros((g, R, n), dtype=dtype), W_uv=torch.zeros((g, R, v), dtype=dtype))
+    pools = dict(k_pool=torch.zeros(lead + ((g * n + r,) if shared else (g, n + r)), dtype=dtype),
+                 v_pool=torch.zeros(lead + (g, v), dtype=dtype))
+    latent = dict(latent=torch.zeros(lead + (R + r,), dtype=dtype))
+    if path == "append":
+        a = dict(dims=d, layout=lay, new_rows=torch.zeros((B, T, R + r), dtype=dtype), sizes=None)
+        return {**a, **latent, **weights, **pools}
+    return {**a, **(pools if path == "gqa" else {**latent, **weights})}
+
+
+@pytest.mark.parametrize("path", ["gqa", "absorb", "append"])
+@pytest.mark.parametrize("page,shared,dtype", [(0, 0, torch.bfloat16), (16, 1, torch.float32)])
+def test_binding_checks_the_attentions_tensors(G, path, page, shared, dtype):
+    """Masks of another tree or batch, and any tensor of another type, size or
+    order, are refused before the library is called."""
+    call = {"gqa": G.gqla_decode_tree_gqa, "absorb": G.gqla_decode_tree_absorb, "append": G.gqla_append_tree}[path]
+    good = _attention_args(G, path, dtype, page, shared)
+    wrong = []
+    for name, t in good.items():
+        if isinstance(t, torch.Tensor):
+            wrong += [(name, t.to(torch.float16)), (name, t[:-1]), (name, t.transpose(0, 1))]
+            if "pool" not in name and name != "latent":
+                wrong.append((name, torch.cat([t, t])))
+    i64 = dict(dtype=torch.int64)
+    if path == "append":
+        wrong += [("sizes", torch.zeros(3, dtype=torch.int32)), ("sizes", torch.zeros(2, **i64))]
+    else:
+        wrong += [("tree", G.make_tree(torch.zeros(shape, **i64))) for shape in ((2, 2), (2, 4), (1, 3), (3, 2))]
+        wrong += [("workspace", torch.zeros((64, 64), dtype=torch.uint8).t())]
+    wrong += [("dev_status", torch.zeros(1, **i64)), ("dev_status", torch.zeros(0, dtype=torch.int32))]
+    for name, t in wrong:
+        with pytest.raises(ValueError):
+            call(**{**good, name: t})
+    # what is right gets past the checks: the library itself refuses these dims
+    good["dims"].scale = float("nan")
+    with pytest.raises(G.GqlaError):
+        call(**good)
