@@ -307,7 +307,9 @@ gqla_status gqla_append_tree(const gqla_dims* dims, const gqla_kv_layout* layout
  * A row that sees nothing and a slot i >= n_b give out = 0, lse = -inf.  Keys
  * that a row does not see do not enter it whatever they hold; value (latent)
  * rows that no row of the sequence sees are not read as values either.  A
- * value seen by some rows must be finite.
+ * value seen by some rows must be finite.  A score that a row sees and that is
+ * NaN or +infinity gives NaN in the row's out and lse; scores that are all
+ * -infinity count as nothing seen.
  *   q         device [B, s_q, n_h, d_nope + d_rope]
  *   out       device [B, s_q, n_h, d_v] (written); lse fp32 [B, s_q, n_h] or NULL
  *   workspace device, >= gqla_tree_workspace_bytes(...), 256-byte aligned;

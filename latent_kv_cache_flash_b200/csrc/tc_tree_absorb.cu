@@ -68,7 +68,7 @@ struct TreeAbsorbParams {
   float* o_lat;                // [batch][units][block]: those that one worker held whole
   float* lse_lat;              // [rows]
   float* o_part;               // [worker][2][block]
-  float* lse_part;             // [worker][2][64]; NaN: the segment met a bad page
+  float* lse_part;             // [worker][2][64]; bad_part(): the segment met a bad page
   int units;                   // row blocks of a sequence's slots
   int merged;                  // tree_latent_merge has joined the parts
   long long* prefix;           // [batch + 2]
@@ -397,7 +397,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&m_ready[gp][qd]);
           if (m_used != m_new) {
-            l_sum = m_used == -INFINITY ? 0.f : l_sum * ptx::fast_exp2(m_used - m_new);
+            // before the first score above -inf the sum is 0, or NaN
+            if (m_used != -INFINITY) l_sum *= ptx::fast_exp2(m_used - m_new);
             m_used = m_new;
           }
           if (m_prev != -INFINITY && m_new != m_prev) factor = ptx::fast_exp2(m_prev - m_new);
@@ -495,9 +496,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g2 = 0; g2 < 2; ++g2) {
           const float lg = row_sum[kM * g2 + row], mg = row_at[kM * g2 + row];
           broken |= lg < 0.f;
-          if (mg != -INFINITY) l += lg * ptx::fast_exp2(mg - mt);
+          l += mg == -INFINITY ? lg : lg * ptx::fast_exp2(mg - mt);
         }
-        const bool none = broken || !(l > 0.f);
+        // NaN where a score was NaN or +inf, or so large that its weight overflows
+        if (l == INFINITY) l = NAN;
+        const bool none = broken || (l == 0.f && mt == -INFINITY);
         const float inv = none ? 0.f : 1.f / l;
         float* dst = block + (long long)row * kR + 4 * half;
 #pragma unroll 1
@@ -520,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (valid && gp == 0 && half == 0) {
-          const float lse = broken ? NAN : none ? -INFINITY : (mt + log2f(l)) * kLn2;
+          const float lse = broken ? bad_part() : none ? -INFINITY : (mt + log2f(l)) * kLn2;
           (whole ? p.lse_lat + grow : p.lse_part + slot * kM + row)[0] = lse;
         }
       }
@@ -584,15 +587,17 @@ __global__ void __launch_bounds__(128) tree_latent_merge(const TreeAbsorbParams 
   const int ur = lr % kM;
   const long long at = (long long)ur * kR + 128 * warp + 4 * lane;
   float mx = -INFINITY, Z = 0.f, z0 = -INFINITY;
-  bool bad = false;
+  bool bad = false, nan = false;
   for (int i = lane; i < u.n; i += 32) {
     const float z = p.lse_part[part_slot(u.first + i, i == 0) * kM + ur];
     if (i < 32) z0 = z;
-    bad |= z != z;
+    bad |= is_bad_part(z);
+    nan |= z != z;
     mx = fmaxf(mx, z);
   }
   mx = warp_max(mx);
   bad = __any_sync(0xffffffffu, bad);
+  if (__any_sync(0xffffffffu, nan)) mx = NAN;        // and so will be the row
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < u.n && !bad && mx != -INFINITY; i0 += 32) {
     const int left = min(32, u.n - i0);
@@ -609,10 +614,10 @@ __global__ void __launch_bounds__(128) tree_latent_merge(const TreeAbsorbParams 
       acc.w = fmaf(w, v.w, acc.w);
     }
   }
-  const float inv = Z > 0.f ? 1.f / Z : 0.f;
+  const float inv = Z != 0.f ? 1.f / Z : 0.f;
   *reinterpret_cast<float4*>(p.o_lat + ((long long)bs * p.units + u.rb) * kBlockFloats + at) =
       make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-  if (threadIdx.x == 0) p.lse_lat[row] = bad ? NAN : Z > 0.f ? mx + logf(Z) : -INFINITY;
+  if (threadIdx.x == 0) p.lse_lat[row] = bad ? bad_part() : Z != 0.f ? mx + logf(Z) : -INFINITY;
 }
 
 template <int kRows, int kN>
@@ -676,16 +681,17 @@ __global__ void __launch_bounds__(up_threads(kRows)) tree_merge_up_kernel(const 
         } else {
           // a lane a part: log-sum-exps and weights, then all lanes the values
           float mx = -INFINITY, Z = 0.f, z0 = -INFINITY;
-          bool bad = false;
+          bool bad = false, nan = false;
           for (int i = lane; i < n; i += 32) {
             const float z = p.lse_part[part_slot(first + i, i == 0) * kM + ur];
             if (i < 32) z0 = z;
-            bad |= z != z;
+            bad |= is_bad_part(z);
+            nan |= z != z;
             mx = fmaxf(mx, z);
           }
           mx = warp_max(mx);
           bad = __any_sync(0xffffffffu, bad);
-          if (bad) lse = NAN;
+          if (__any_sync(0xffffffffu, nan)) mx = NAN;
           for (int i0 = 0; i0 < n && !bad && mx != -INFINITY; i0 += 32) {
             const int left = min(32, n - i0);
             if (i0 > 0) z0 = lane < left ? p.lse_part[part_slot(first + i0 + lane, false) * kM + ur] : -INFINITY;
@@ -706,7 +712,7 @@ __global__ void __launch_bounds__(up_threads(kRows)) tree_merge_up_kernel(const 
               }
             }
           }
-          if (Z > 0.f) {
+          if (Z != 0.f) {
             const float inv = 1.f / Z;
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4)
@@ -714,7 +720,7 @@ __global__ void __launch_bounds__(up_threads(kRows)) tree_merge_up_kernel(const 
             lse = mx + logf(Z);
           }
         }
-        if (lse != lse) lse = -INFINITY;       // a bad page: its values are zeros
+        if (is_bad_part(lse)) lse = -INFINITY; // a bad page: its values are zeros
       }
       if (lane == 0 && lse_out && n0 == 0) lse_out[row] = lse;
     }

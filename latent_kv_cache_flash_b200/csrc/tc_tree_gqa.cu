@@ -70,7 +70,7 @@ struct TreeGqaParams {
   __nv_bfloat16* out;
   float* lse;          // or nullptr
   float* o_part;       // [worker][2][row_block][128]
-  float* lse_part;     // [worker][2][row_block]; NaN: the segment met a bad page
+  float* lse_part;     // [worker][2][row_block]; bad_part(): the segment met a bad page
   long long* prefix;   // [batch + 2]
   int n_h, G, m;
   KRow kr;
@@ -484,7 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&m_ready[gp][qd]);
           if (m_used != m_new) {
-            l_sum = m_used == -INFINITY ? 0.f : l_sum * ptx::fast_exp2(m_used - m_new);
+            // before the first score above -inf the sum is 0, or NaN
+            if (m_used != -INFINITY) l_sum *= ptx::fast_exp2(m_used - m_new);
             m_used = m_new;
           }
           const bool grew = m_prev != -INFINITY && m_new != m_prev;
@@ -571,9 +572,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int g2 = 0; g2 < 2; ++g2) {
           const float lg = row_sum[g2][row], mg = row_at[g2][row];
           broken |= lg < 0.f;
-          if (mg != -INFINITY) l += lg * ptx::fast_exp2(mg - mt);
+          l += mg == -INFINITY ? lg : lg * ptx::fast_exp2(mg - mt);
         }
-        const bool none = broken || !(l > 0.f);
+        // NaN where a score was NaN or +inf, or so large that its weight overflows
+        if (l == INFINITY) l = NAN;
+        const bool none = broken || (l == 0.f && mt == -INFINITY);
         const float inv = none ? 0.f : 1.f / l;
         const bool whole = cur.n == cur.tiles;
         const int used = cur.nt.n * p.m - cur.rb * C::kRows - kM * (int)rank;
@@ -616,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (valid && gp == 0) {
           const float lse = none ? -INFINITY : (mt + log2f(l)) * kLn2;
-          if (!whole) p.lse_part[prow] = broken ? NAN : lse;
+          if (!whole) p.lse_part[prow] = broken ? bad_part() : lse;
           else if (p.lse) p.lse[grow] = lse;
         }
       }
@@ -666,15 +669,17 @@ __global__ void __launch_bounds__(256) tree_gqa_merge(const TreeGqaParams p) {
     const int rr = r % p.work.row_block;
     // a lane a part: log-sum-exps and weights, then all lanes the values
     float mx = -INFINITY, Z = 0.f, z0 = -INFINITY;
-    bool bad = false;
+    bool bad = false, nan = false;
     for (int i = lane; i < u.n; i += 32) {
       const float z = p.lse_part[part_slot(u.first + i, i == 0) * p.work.row_block + rr];
       if (i < 32) z0 = z;
-      bad |= z != z;
+      bad |= is_bad_part(z);
+      nan |= z != z;
       mx = fmaxf(mx, z);
     }
     mx = warp_max(mx);
     bad = __any_sync(0xffffffffu, bad);
+    if (__any_sync(0xffffffffu, nan)) mx = NAN;      // and so will be the row
     for (int i0 = 0; i0 < u.n && !bad && mx != -INFINITY; i0 += 32) {
       const int left = min(32, u.n - i0);
       if (i0 > 0)
@@ -692,7 +697,7 @@ __global__ void __launch_bounds__(256) tree_gqa_merge(const TreeGqaParams p) {
         acc.w = fmaf(w, v.w, acc.w);
       }
     }
-    if (Z > 0.f) {
+    if (Z != 0.f) {
       const float inv = 1.f / Z;
       acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
       lse = mx + logf(Z);

@@ -229,9 +229,10 @@ __global__ void __launch_bounds__(kThreads, kU == 1 ? 3 : kU == 2 ? 2 : 1)
     const int r = r0 + 2 * ty + a;
     if (r >= p.s_q * p.m) continue;
     const long long row = split * p.rows + grow_of(r);
-    if (tx == 0) p.lse_part[row] = l[a] > 0.f ? mx[a] + logf(l[a]) : -INFINITY;
+    // a sum of 0: nothing seen; of NaN: a score was NaN or +inf, and so are the outputs
+    if (tx == 0) p.lse_part[row] = l[a] != 0.f ? mx[a] + logf(l[a]) : -INFINITY;
     if (r >= rows_used) continue;
-    const float inv = l[a] > 0.f ? 1.f / l[a] : 0.f;
+    const float inv = l[a] != 0.f ? 1.f / l[a] : 0.f;
 #pragma unroll
     for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -252,12 +253,15 @@ __global__ void __launch_bounds__(128) tree_simt_merge(int S, long long rows, in
   const int lane = threadIdx.x & 31;
   if (row >= rows) return;
   float mx = -INFINITY, z0 = -INFINITY;
+  bool nan = false;
   for (int i = lane; i < S; i += 32) {
     const float z = lse_part[i * rows + row];
     if (i < 32) z0 = z;
+    nan |= z != z;
     mx = fmaxf(mx, z);
   }
   mx = warp_max(mx);
+  if (__any_sync(0xffffffffu, nan)) mx = NAN;        // and so will be the row
   float Z = 0.f;
   for (int c0 = 0; c0 < dv; c0 += 128) {         // 4 columns a lane at a time
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
@@ -278,12 +282,12 @@ __global__ void __launch_bounds__(128) tree_simt_merge(int S, long long rows, in
           if (w != 0.f && c0 + lane + 32 * k < dv) acc[k] = fmaf(w, src[lane + 32 * k], acc[k]);
       }
     }
-    const float inv = Z > 0.f ? 1.f / Z : 0.f;
+    const float inv = Z != 0.f ? 1.f / Z : 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (c0 + lane + 32 * k < dv) out[row * dv + c0 + lane + 32 * k] = from_f32<T>(acc[k] * inv);
   }
-  if (lane == 0 && lse_out) lse_out[row] = Z > 0.f ? mx + logf(Z) : -INFINITY;
+  if (lane == 0 && lse_out) lse_out[row] = Z != 0.f ? mx + logf(Z) : -INFINITY;
 }
 
 // The latent form's two products, q~ = W_uk^g q_nope and out = o~ W_uv^g: 32

@@ -187,6 +187,12 @@ __device__ __forceinline__ void share_start(const TreeWork& w, const KvLayout& l
 // the unit is whole and was written to the output.
 __device__ __forceinline__ long long part_slot(long long worker, bool begins) { return 2 * worker + (begins ? 1 : 0); }
 
+// The log-sum-exp of a part that met a bad page, whose row is zeros.  A NaN of
+// its own: arithmetic gives the one with all bits set, which stands for rows
+// with a score of NaN or +inf.
+__device__ __forceinline__ float bad_part() { return __uint_as_float(0x7fc00bad); }
+__device__ __forceinline__ bool is_bad_part(float lse) { return __float_as_uint(lse) == 0x7fc00bad; }
+
 // The batch's list as the merge needs it, in a warp's lanes: lane b has sequence
 // b's.  With up to 32 sequences it needs the lengths only, which the attention
 // kernel does not write: the merge then makes it, and fetches its code, while
