@@ -383,8 +383,9 @@ struct SimtPlan {
   size_t qt, o_lat, o_part, lse_part, bytes;
 };
 
-// Blocks for four waves of the SMs, in tiles of 64 tokens; a requested count is
-// honoured up to that.
+// Splits of whole tiles of 64 tokens.  The library's choice: blocks for four
+// waves of the SMs, 64 splits at most; a requested count is honoured up to the
+// number of tiles and to 256.
 SimtPlan plan_of(const Problem& p, gqla_path path, int requested) {
   SimtPlan w;
   const bool lat = path == GQLA_PATH_ABSORB;
@@ -398,8 +399,10 @@ SimtPlan plan_of(const Problem& p, gqla_path path, int requested) {
   const long long slots = p.ly.page_size == 0 ? p.ly.capacity : (long long)p.ly.mbps * p.ly.page_size;
   const long long tiles = ((p.ly.max_seq_len < slots ? p.ly.max_seq_len : slots) + kTok - 1) / kTok;
   long long S = requested > 0 ? requested : 4LL * num_sms() / units;
-  S = S < 1 ? 1 : S > 64 && requested <= 0 ? 64 : S;
-  S = S > tiles ? tiles : S > 256 ? 256 : S;
+  const long long most = requested > 0 ? 256 : 64;
+  S = S > most ? most : S;
+  S = S > tiles ? tiles : S;
+  S = S < 1 ? 1 : S;
   const long long per = (tiles + S - 1) / S;
   w.splits = (int)((tiles + per - 1) / per);
   w.chunk = per * kTok;

@@ -221,3 +221,19 @@ def test_binding_checks_the_attentions_tensors(G, path, page, shared, dtype):
     good["dims"].scale = float("nan")
     with pytest.raises(G.GqlaError):
         call(**good)
+
+
+def test_a_requested_split_count_has_a_limit(G):
+    """256 splits at most, however many tiles there are and more are asked for,
+    and no more workspace for asking; the library's own choice is 64 at most."""
+    for L in (64000, 10 ** 6, 2 ** 31 - 1):
+        _, lay = _layout(G, B=1, L=L)
+        d = _dims(G, n_h=2, G=2, d_nope=16, d_rope=8, d_v=16, r=32, s_q=2, dtype=G.GQLA_F32)
+        for path in (G.GQLA_PATH_GQA, G.GQLA_PATH_ABSORB):
+            counts = [G.gqla_tree_num_splits(d, lay, n, path) for n in (1, 255, 256, 257, 900, 2000, 2 ** 31 - 1)]
+            assert counts[0] == 1 and max(counts) <= 256 and counts == sorted(counts)
+            assert len({G.gqla_tree_workspace_bytes(d, lay, n, path) for n in (256, 900, 2000, 2 ** 31 - 1)}) == 1
+            assert 1 <= G.gqla_tree_num_splits(d, lay, 0, path) <= 64
+    # fewer tiles than asked for
+    _, lay = _layout(G, B=1, L=130)
+    assert G.gqla_tree_num_splits(d, lay, 2000, G.GQLA_PATH_GQA) == 3
