@@ -48,13 +48,12 @@ __device__ __forceinline__ NewTokens new_tokens(const KvLayout& ly, const TreeVi
 
 // New tokens that new token i of sequence b sees (bit j: the j-th), i < nt.n.
 __device__ __forceinline__ uint64_t new_mask(const TreeView& tr, const NewTokens& nt, int b, int s_q, int i) {
-  return tr.on ? tr.masks[(long long)b * s_q + i] & low_bits(nt.n) : low_bits(i + 1);
+  return tr.masks[(long long)b * s_q + i] & low_bits(nt.n);
 }
 
 // New tokens that at least one of the sequence's new tokens sees.  All 32
 // lanes of a warp call it.
 __device__ __forceinline__ uint64_t new_union(const TreeView& tr, const NewTokens& nt, int b, int s_q) {
-  if (!tr.on) return low_bits(nt.n);
   uint64_t u = 0;
   for (int i = threadIdx.x & 31; i < nt.n; i += 32) u |= tr.masks[(long long)b * s_q + i];
   const uint32_t lo = __reduce_or_sync(0xffffffffu, (uint32_t)u), hi = __reduce_or_sync(0xffffffffu, (uint32_t)(u >> 32));
