@@ -357,7 +357,9 @@ int32_t gqla_tree_num_splits(const gqla_dims* dims, const gqla_kv_layout* layout
  *   target, draft    device, row b * n_tokens + i at a pitch of target_pitch
  *                    (draft_pitch) elements >= vocab, of probs_dtype: the
  *                    probabilities after token i.  Rows of draft are read for
- *                    tokens with children only; draft may be NULL
+ *                    tokens with children only; draft may be NULL.  Rows may
+ *                    start anywhere; where a token's two rows lie differently
+ *                    to 16-byte boundaries the call takes about a quarter more
  *   u_accept         device fp32 [batch, n_tokens] (the root's is not read)
  *   u_sample         device fp32 [batch]
  *   accepted         device [batch, n_tokens] (written): the path's token

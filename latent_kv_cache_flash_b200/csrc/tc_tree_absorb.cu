@@ -12,8 +12,11 @@
 // 16-31 hold O (2 x 256 columns), lanes 0-15 Q~ (288) and two S (2 x 64).
 // M = 64 runs the tensor pipe at half its rate (64 cycles for N = 128, K = 16,
 // 4096 of 8192 flop a cycle).  M = 128 over a pair of CTAs has the full rate
-// but would stage a tile's rows twice, for the scores by token and for the
-// values by column: per row the same shared-memory fill, and more than fits.
+// but, loaded as here, would stage a tile's rows twice, for the scores by token
+// and for the values by column: 36 + 32 KB of a tile of 64 tokens a CTA for 64
+// rows, where this form takes 72 KB, and O (256 columns) with two S (64) leaves
+// 192 of 512 columns for Q~, which needs 288.  Counted, not built; halves passed
+// between the CTAs of a pair, and a part of Q~ in shared memory, are open.
 // A tile of 64 tokens costs the pipe 2176 cycles.
 //
 // One persistent CTA an SM takes a share of the batch's tile list
@@ -889,7 +892,8 @@ cudaError_t tc_tree_absorb(const Problem& p, const TreeView& tree, const void* q
   count_launch();
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // parts of a row, as far as the host can tell
+  // parts of a row, as far as the host can tell: a max_seq_len far above the
+  // lengths brings the extra pass to short contexts too
   const long long units = (long long)p.ly.batch * prm.units, tiles = ((long long)p.ly.max_seq_len + kT - 1) / kT;
   const long long parts = prm.work.workers / units < tiles ? prm.work.workers / units : tiles;
   prm.merged = parts > 5;

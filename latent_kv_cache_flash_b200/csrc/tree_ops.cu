@@ -66,9 +66,11 @@ __global__ void __launch_bounds__(kMaxTree) tree_masks_kernel(int n_tokens, cons
 // Sums are in 64 bits: the rows have up to some 10^5 terms, and a draw next to
 // a border must not depend on how they are grouped.
 // Bound by the passes' latencies, one after the other (loads, 64-bit sums, the
-// exchange: about 2 us each).  64 trees of 24 over 128000 fp32: 49 us, of which
-// the rows' bytes would take 10; 16 of 16 over 100003 bf16: 19.5; one of 6 over
-// 32000: 6.4.
+// exchange: about 2 us each).  64 trees of 24 over 128000 fp32: 49..52 us, of
+// which the rows' bytes would take 10; 16 of 16 over 100003 bf16: 19.5..21.6; one
+// of 6 over 32000: 6.4..6.8 (several boxes and seeds).  Where rows of target and
+// draft lie differently to 16-byte boundaries a residual's sums go element by
+// element: 62 for 50 us, 23.9 for 19.8.
 constexpr int kVWarps = 16;
 constexpr int kVThreads = kVWarps * 32;
 constexpr int kMaxCluster = 8;
@@ -668,16 +670,17 @@ cudaError_t verify_tree(int batch, int n_tokens, int vocab, const int32_t* paren
                  u_accept, u_sample, accepted, n_accepted, next_token, st};
   // CTAs per sequence, as long as every warp keeps two loads a lane: a
   // sequence's passes follow one another, and the one with the most of them
-  // decides the time, so up to four times what the GPU holds at once.  For 64
-  // sequences over 128000 fp32 it makes little difference (8 a sequence 55 us,
-  // 4 56); one over 32000 takes 6.5 us with 8
+  // decides the time, so up to four times what the GPU holds at once.  With 8
+  // and with 4 at most: 64 sequences over 128000 fp32, 8 of which are two waves,
+  // 51.9 and 59.5 us (bf16 45.6 and 50.1); 16 over 100003 bf16 21.6 and 26.0; one
+  // over 32000 fp32 6.8 and 7.5
   const int groups = vocab / (dtype == GQLA_F32 ? 4 : 8);
   int C = 1;
   while (C < kMaxCluster && 2 * C * kVThreads * 2 <= groups && (long long)batch * C * 2 <= 8LL * num_sms()) C *= 2;
-  // Rows stay in registers where they fit and a CTA an SM holds the batch (16
-  // sequences over 100003 bf16: 20.6 us, streamed again each pass 24.2, both with
-  // a cluster barrier a pass); with
-  // more, two CTAs an SM hide each other's latencies.
+  // Rows stay in registers where they fit and a CTA an SM holds the batch: held,
+  // and streamed again each pass, 8 sequences over 128000 fp32 take 17.1 and 18.9
+  // us, one over 32000 6.8 and 7.5, 16 over 100003 bf16, which fill the SMs, 21.6
+  // and 21.3.  With more, two CTAs an SM hide each other's latencies.
   const bool keep = (long long)batch * C <= num_sms() && groups + 2 <= (long long)C * kVWarps * 32 * kVKeep;
   if (dtype == GQLA_F32)
     return draft ? launch_verify<float, false>(p, batch, C, keep, s) : launch_verify<float, true>(p, batch, C, keep, s);
