@@ -267,6 +267,8 @@ gqla_status gqla_splitkv_combine(int32_t num_splits, int32_t rows, int32_t D,
  *   gqla_append_tree, gqla_decode_tree_*  per layer
  *   gqla_verify_tree, gqla_commit_tree    once
  *
+ * Arrays of lengths, sizes, indices, masks and random numbers, and *dev_status,
+ * start at a multiple of their elements' size (else GQLA_ERR_ALIGNMENT).
  * What slots i >= n_b of q, new_rows and the other per-slot inputs hold does
  * not matter (they may be read, and reach no result). */
 #define GQLA_MAX_TREE 64

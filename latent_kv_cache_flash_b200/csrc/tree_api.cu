@@ -9,6 +9,11 @@ using namespace gqla;
 namespace {
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+// Pointers to 4-byte elements; nullptr is aligned.
+template <typename... P>
+bool aligned4(const P*... p) {
+  return ((... | (uintptr_t)p) & 3u) == 0;
+}
 
 gqla_status check_layout(const gqla_kv_layout* l) {
   if (!l || !l->seq_lens) return GQLA_ERR_INVALID_ARG;
@@ -56,6 +61,8 @@ gqla_status decode_tree(const gqla_dims* dims, const gqla_kv_layout* layout, con
   if (!q || !k_pool || !v_pool || !out || (lat && (!W_uk || !W_uv))) return GQLA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out)) return GQLA_ERR_ALIGNMENT;
   if (lat && (!aligned16(W_uk) || !aligned16(W_uv))) return GQLA_ERR_ALIGNMENT;
+  if (((uintptr_t)tree->masks & 7u) || !aligned4(tree->sizes, lse, dev_status, layout->seq_lens, layout->block_table))
+    return GQLA_ERR_ALIGNMENT;
   const bool tc = on_tensor_cores(p, path);
   if (!tc && (!simt_supports(p, path) || p.rows >= (1LL << 31) || p.d.G > 65535)) return GQLA_ERR_UNSUPPORTED;
   const size_t need = workspace_of(p, path, num_splits);
@@ -86,6 +93,7 @@ gqla_status gqla_append_tree(const gqla_dims* dims, const gqla_kv_layout* layout
   if (!aligned16(new_rows) || (latent && !aligned16(latent))) return GQLA_ERR_ALIGNMENT;
   if (expand && (!aligned16(W_uk) || !aligned16(W_uv) || !aligned16(k_pool) || !aligned16(v_pool)))
     return GQLA_ERR_ALIGNMENT;
+  if (!aligned4(sizes, dev_status, layout->seq_lens, layout->block_table)) return GQLA_ERR_ALIGNMENT;
   // without a latent pool the expansion must read the dense new rows
   if (!latent && !tc_expand_supports(p)) return GQLA_ERR_UNSUPPORTED;
   const TreeView v{1, nullptr, sizes};
@@ -133,6 +141,7 @@ int32_t gqla_tree_num_splits(const gqla_dims* dims, const gqla_kv_layout* layout
 gqla_status gqla_tree_masks(int32_t batch, int32_t n_tokens, const int32_t* parents, const int32_t* sizes,
                             uint64_t* masks, int32_t* dev_status, void* stream) {
   if (batch < 1 || n_tokens < 1 || n_tokens > GQLA_MAX_TREE || !parents || !masks) return GQLA_ERR_INVALID_ARG;
+  if (((uintptr_t)masks & 7u) || !aligned4(parents, sizes, dev_status)) return GQLA_ERR_ALIGNMENT;
   const cudaError_t e = tree_masks(batch, n_tokens, parents, sizes, masks, dev_status, (cudaStream_t)stream);
   return e == cudaSuccess ? GQLA_OK : GQLA_ERR_CUDA;
 }
@@ -150,6 +159,8 @@ gqla_status gqla_verify_tree(int32_t batch, int32_t n_tokens, int32_t vocab, con
   // rows may start anywhere (an odd vocabulary), elements not
   const uintptr_t el = probs_dtype == GQLA_F32 ? 3 : 1;
   if (((uintptr_t)target & el) || ((uintptr_t)draft & el)) return GQLA_ERR_ALIGNMENT;
+  if (!aligned4(parents, sizes, tokens, u_accept, u_sample, accepted, n_accepted, next_token, dev_status))
+    return GQLA_ERR_ALIGNMENT;
   if (batch > (1 << 24) || vocab > (1 << 30)) return GQLA_ERR_UNSUPPORTED;
   const cudaError_t e = verify_tree(batch, n_tokens, vocab, parents, sizes, tokens, target, target_pitch, draft,
                                     draft_pitch, probs_dtype, u_accept, u_sample, accepted, n_accepted, next_token,
@@ -170,6 +181,8 @@ gqla_status gqla_commit_tree(const gqla_kv_layout* layout, int32_t n_tokens, con
     if (((uintptr_t)pools[i].base & 1) || (pools[i].row_bytes & 1)) return GQLA_ERR_ALIGNMENT;
     if (pools[i].row_bytes > (1 << 30)) return GQLA_ERR_UNSUPPORTED;
   }
+  if (!aligned4(sizes, accepted, n_accepted, seq_lens_out, dev_status, layout->seq_lens, layout->block_table))
+    return GQLA_ERR_ALIGNMENT;
   const KvLayout ly{layout->seq_lens, layout->block_table, layout->batch, layout->max_seq_len, layout->page_size,
                     layout->page_size == 0 ? layout->capacity : layout->max_blocks_per_seq * layout->page_size,
                     layout->max_blocks_per_seq, layout->num_pages};

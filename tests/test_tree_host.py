@@ -237,3 +237,35 @@ def test_a_requested_split_count_has_a_limit(G):
     # fewer tiles than asked for
     _, lay = _layout(G, B=1, L=130)
     assert G.gqla_tree_num_splits(d, lay, 2000, G.GQLA_PATH_GQA) == 3
+
+
+def test_arrays_off_their_elements_size_are_refused(G):
+    """A read of them would be a misaligned access on the device."""
+    L, p = G.lib(), ctypes.byref
+    at = lambda off: ctypes.c_void_p(0x10000 + off)     # noqa: E731
+    off2, off4 = at(2), at(4)
+    no = G.GQLA_ERR_ALIGNMENT
+    lens, lay = _layout(G)
+    d = _dims(G)
+    far = _layout(G)[1]
+    far.seq_lens = 0x10002
+    for call in (lambda t=p(G.GqlaTree(at(0), None)), lse=None, st=None, lay=lay:
+                 L.gqla_decode_tree_gqa(p(d), p(lay), t, A, A, A, A, lse, 0, A, 1 << 34, st, None),
+                 lambda t=p(G.GqlaTree(at(0), None)), lse=None, st=None, lay=lay:
+                 L.gqla_decode_tree_absorb(p(d), p(lay), t, A, A, A, A, A, lse, 0, A, 1 << 34, st, None)):
+        for kw in (dict(t=p(G.GqlaTree(off4, None))), dict(t=p(G.GqlaTree(A, off2))), dict(lse=off2), dict(st=off2), dict(lay=far)):
+            assert call(**kw) == no, kw
+    assert L.gqla_append_tree(p(d), p(lay), off2, A, A, A, A, A, A, None, None) == no
+    assert L.gqla_append_tree(p(d), p(lay), None, A, A, A, A, A, A, off2, None) == no
+    assert L.gqla_append_tree(p(d), p(far), None, A, A, A, A, A, A, None, None) == no
+    for args in ((off2, None, A, None), (A, off2, A, None), (A, None, off4, None), (A, None, A, off2)):
+        assert L.gqla_tree_masks(2, 4, *args, None) == no
+    good = [A, A, A, A, 100, A, 100, 0, A, A, A, A, A, A]
+    for i in (0, 1, 2, 8, 9, 10, 11, 12, 13):
+        args = list(good)
+        args[i] = off2
+        assert L.gqla_verify_tree(2, 4, 100, *args, None) == no, i
+    pool = (G.GqlaPool * 1)(G.GqlaPool(0x10000, 64))
+    for sizes, acc, n, out, st, l in ((off2, A, A, A, None, lay), (None, off2, A, A, None, lay), (None, A, off2, A, None, lay),
+                                      (None, A, A, off2, None, lay), (None, A, A, A, off2, lay), (None, A, A, A, None, far)):
+        assert L.gqla_commit_tree(p(l), 4, sizes, acc, n, pool, 1, out, st, None) == no
